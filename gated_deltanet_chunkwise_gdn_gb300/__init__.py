@@ -19,6 +19,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
+from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, kept_workspace, workspace_lock, workspace_of
 from ._lib import GdnError
 from .mixer import (CausalConv, GdnConvGrads, GdnNormGrads, GdnSsmGrads, LayerNorm, SelectiveScan, gdn_conv_backward,
                     gdn_conv_extend, gdn_conv_step, gdn_layer_norm, gdn_layer_norm_backward, gdn_ssm_backward,
@@ -31,7 +32,6 @@ __all__ = ["gdn_extend_chunkwise", "gdn_decode_step", "gdn_chunkwise_backward", 
            "gdn_ssm_extend", "gdn_ssm_step", "gdn_ssm_backward", "GdnSsmGrads", "SelectiveScan",
            "gdn_layer_norm", "gdn_layer_norm_backward", "GdnNormGrads", "LayerNorm"]
 
-_ws_cache: dict = {}
 _status_cache: dict = {}
 
 
@@ -45,28 +45,6 @@ def version() -> int:
 
 def gdn_workspace_size(total_tokens: int, batch: int, H: int, HV: int, K: int, V: int, chunk_size: int) -> int:
     return int(_lib.load().gdn_workspace_size(total_tokens, batch, H, HV, K, V, chunk_size))
-
-
-def _workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int) -> torch.Tensor:
-    """The cached workspace of (device, stream).
-
-    One buffer per stream: calls on one stream are ordered, so they may share it, while calls
-    on two streams of a device run concurrently and must not. The buffer is allocated on the
-    call's stream, so when it is replaced by a larger one, the caching allocator reuses the old
-    memory only in that stream's order, after the calls already enqueued there.
-    """
-    key = (device.index, stream.cuda_stream)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        with torch.cuda.stream(stream):
-            buf = torch.empty(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
-        _ws_cache[key] = buf
-    return buf
-
-
-def _aligned_ptr(buf: torch.Tensor) -> int:
-    p = buf.data_ptr()
-    return (p + 255) & ~255
 
 
 def _req(t: torch.Tensor, name: str, dtype, device):
@@ -128,20 +106,23 @@ def gdn_extend_chunkwise(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indice
     elif not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     sp = stream.cuda_stream
+    lock = UNSHARED
     if workspace is None:
-        ws = _workspace(dev, stream, need)
+        ws = kept_workspace(dev, stream, need)
         ws_ptr, ws_bytes = _aligned_ptr(ws), ws.numel() - (_aligned_ptr(ws) - ws.data_ptr())
+        lock = workspace_lock(dev, sp)
     else:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     dtype_code = _lib.GDN_BF16 if q.dtype == torch.bfloat16 else _lib.GDN_FP16
-    st = L.gdn_extend_chunkwise(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_code,
-        a.data_ptr(), b.data_ptr(), A_log.data_ptr(), dt_bias.data_ptr(),
-        state_pool.data_ptr(), state_pool.shape[0], cache_indices.data_ptr(), cu_seqlens.data_ptr(), B,
-        out.data_ptr(), T, H, HV, K, V, int(chunk_size), float(scale), ws_ptr, ws_bytes, sp)
-    _lib.check(st, "gdn_extend_chunkwise")
-    if check:
-        _lib.check(L.gdn_get_device_status(ws_ptr, sp), "gdn_extend_chunkwise (device)")
+    with lock:
+        st = L.gdn_extend_chunkwise(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_code,
+            a.data_ptr(), b.data_ptr(), A_log.data_ptr(), dt_bias.data_ptr(),
+            state_pool.data_ptr(), state_pool.shape[0], cache_indices.data_ptr(), cu_seqlens.data_ptr(), B,
+            out.data_ptr(), T, H, HV, K, V, int(chunk_size), float(scale), ws_ptr, ws_bytes, sp)
+        _lib.check(st, "gdn_extend_chunkwise")
+        if check:
+            _lib.check(L.gdn_get_device_status(ws_ptr, sp), "gdn_extend_chunkwise (device)")
     return out
 
 
@@ -353,7 +334,7 @@ def gdn_get_device_status(device=None, stream=None) -> int:
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else torch.device(device).index)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
-    ws = _ws_cache.get((dev.index, stream.cuda_stream))
+    ws = workspace_of(dev.index, stream.cuda_stream)
     if ws is None:
         return 0
     return int(_lib.load().gdn_get_device_status(_aligned_ptr(ws), stream.cuda_stream))

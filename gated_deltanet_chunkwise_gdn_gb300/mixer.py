@@ -9,15 +9,13 @@ they may be column slices of wider projections. Parameters and the scan's states
 
 from __future__ import annotations
 
-import sys
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _lib
+from ._buffers import UNSHARED, aligned_ptr, kept_workspace, workspace_lock
 from ._lib import GdnError
-
-_package = sys.modules[__package__]  # its workspaces, one per stream, serve these calls too
 
 _DTYPE_CODE = {torch.bfloat16: _lib.GDN_BF16, torch.float16: _lib.GDN_FP16, torch.float32: _lib.GDN_FP32}
 
@@ -162,20 +160,19 @@ def _pool(pool, name, dtype, dev, inner):
 
 
 def _workspace(need, what, workspace, stream, handle, dev, keep):
-    """(pointer, bytes, owner) of the call's workspace: the caller's, the one kept for this stream, or a new one."""
+    """(pointer, bytes, owner, lock to hold while the call is enqueued) of the call's workspace: the caller's, the one
+    kept for this stream, or a new one."""
     if need == 0:
         raise GdnError(2, f"{what}: unsupported sizes")
     if workspace is not None:
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace, UNSHARED
     if keep:
-        buf = _package._ws_cache.get((dev.index, handle))
-        if buf is None or buf.numel() < need + 256:
-            buf = _package._workspace(dev, torch.cuda.current_stream(dev) if stream is None else stream, need)
+        buf = kept_workspace(dev, torch.cuda.current_stream(dev) if stream is None else stream, need)
+        lock = workspace_lock(dev, handle)
     else:
-        buf = _empty((need + 256,), torch.uint8, dev, stream)
-    base = buf.data_ptr()
-    ptr = (base + 255) & ~255
-    return ptr, buf.numel() - (ptr - base), buf
+        buf, lock = _empty((need + 256,), torch.uint8, dev, stream), UNSHARED
+    ptr = aligned_ptr(buf)
+    return ptr, buf.numel() - (ptr - buf.data_ptr()), buf, lock
 
 
 def _status_word(status, dev):
@@ -247,9 +244,11 @@ def gdn_conv_extend(x, weight, bias, conv_pool, cache_indices, cu_seqlens, *, ac
     stream, handle = _stream(stream, dev)
     out = _out(out, x, dtype, dev, stream)
     L = _lib.load()
-    ws, nbytes, _keep = _workspace(L.gdn_conv_workspace_size(T, B, D, W), "gdn_conv_extend", workspace, stream, handle, dev, True)
-    st = L.gdn_conv_extend(*args, cp, B, out.data_ptr(), T, D, W, silu, ws, nbytes, handle)
-    _finish(st, "gdn_conv_extend", check, ws, handle)
+    ws, nbytes, _keep, lock = _workspace(L.gdn_conv_workspace_size(T, B, D, W), "gdn_conv_extend", workspace, stream, handle,
+                                         dev, True)
+    with lock:
+        st = L.gdn_conv_extend(*args, cp, B, out.data_ptr(), T, D, W, silu, ws, nbytes, handle)
+        _finish(st, "gdn_conv_extend", check, ws, handle)
     return out
 
 
@@ -296,12 +295,13 @@ def gdn_conv_backward(x, weight, bias, conv_pool, cache_indices, cu_seqlens, d_o
     g = GdnConvGrads(_like(x, stream), _like(weight, stream), None if bias is None else _like(bias, stream),
                      _state_grad(conv_pool, pool, B, dev, stream))
     L = _lib.load()
-    ws, nbytes, _keep = _workspace(L.gdn_conv_backward_workspace_size(T, B, D, W), "gdn_conv_backward", workspace, stream, handle,
-                                   dev, True)
-    st = L.gdn_conv_backward(*args, cp, B, d_out.data_ptr(), ds, dsp,
-                             g.dx.data_ptr(), g.dweight.data_ptr(), None if g.dbias is None else g.dbias.data_ptr(),
-                             g.d_state_pool.data_ptr(), T, D, W, silu, ws, nbytes, handle)
-    _finish(st, "gdn_conv_backward", check, ws, handle)
+    ws, nbytes, _keep, lock = _workspace(L.gdn_conv_backward_workspace_size(T, B, D, W), "gdn_conv_backward", workspace, stream,
+                                         handle, dev, True)
+    with lock:
+        st = L.gdn_conv_backward(*args, cp, B, d_out.data_ptr(), ds, dsp,
+                                 g.dx.data_ptr(), g.dweight.data_ptr(), None if g.dbias is None else g.dbias.data_ptr(),
+                                 g.d_state_pool.data_ptr(), T, D, W, silu, ws, nbytes, handle)
+        _finish(st, "gdn_conv_backward", check, ws, handle)
     return g
 
 
@@ -377,9 +377,11 @@ def gdn_ssm_extend(x, dt, A, B, C, D, z, dt_bias, state_pool, cache_indices, cu_
     stream, handle = _stream(stream, dev)
     out = _out(out, x, dtype, dev, stream)
     L = _lib.load()
-    ws, nbytes, _keep = _workspace(L.gdn_ssm_workspace_size(T, nb, Dm, G, N), "gdn_ssm_extend", workspace, stream, handle, dev, True)
-    st = L.gdn_ssm_extend(*args, cp, nb, out.data_ptr(), T, Dm, G, N, 1 if softplus else 0, ws, nbytes, handle)
-    _finish(st, "gdn_ssm_extend", check, ws, handle)
+    ws, nbytes, _keep, lock = _workspace(L.gdn_ssm_workspace_size(T, nb, Dm, G, N), "gdn_ssm_extend", workspace, stream, handle,
+                                         dev, True)
+    with lock:
+        st = L.gdn_ssm_extend(*args, cp, nb, out.data_ptr(), T, Dm, G, N, 1 if softplus else 0, ws, nbytes, handle)
+        _finish(st, "gdn_ssm_extend", check, ws, handle)
     return out
 
 
@@ -434,8 +436,8 @@ def gdn_ssm_backward(x, dt, A, B, C, D, z, dt_bias, state_pool, cache_indices, c
                     None if dt_bias is None else _like(dt_bias, stream),
                     _state_grad(state_pool, pool, nb, dev, stream) if d_state_pool is None else d_state_pool)
     L = _lib.load()
-    ws, nbytes, _keep = _workspace(L.gdn_ssm_backward_workspace_size(T, nb, Dm, G, N), "gdn_ssm_backward", workspace, stream,
-                                   handle, dev, False)
+    ws, nbytes, _keep, _ = _workspace(L.gdn_ssm_backward_workspace_size(T, nb, Dm, G, N), "gdn_ssm_backward", workspace, stream,
+                                      handle, dev, False)
     st = L.gdn_ssm_backward(*args, cp, nb, d_out.data_ptr(), ds, dsp,
                             *[None if t is None else t.data_ptr() for t in g], T, Dm, G, N, 1 if softplus else 0, ws, nbytes,
                             handle)
@@ -509,8 +511,8 @@ def gdn_layer_norm_backward(d_out, x, weight, mean, rstd, *, workspace: torch.Te
     g = GdnNormGrads(_like(x, stream), dw, db)
     L = _lib.load()
     # (Not the stream's kept workspace: that one's first word is the status of the last call that has one.)
-    ws, nbytes, _keep = _workspace(L.gdn_layer_norm_backward_workspace_size(rows, n), "gdn_layer_norm_backward", workspace,
-                                   stream, handle, dev, False)
+    ws, nbytes, _keep, _ = _workspace(L.gdn_layer_norm_backward_workspace_size(rows, n), "gdn_layer_norm_backward", workspace,
+                                      stream, handle, dev, False)
     st = L.gdn_layer_norm_backward(d_out.data_ptr(), ds, x.data_ptr(), xs, _DTYPE_CODE[dtype], wp, mp, rp, g.dx.data_ptr(),
                                    g.dweight.data_ptr(), g.dbias.data_ptr(), rows, n, ws, nbytes, handle)
     _lib.check(st, "gdn_layer_norm_backward")

@@ -1,0 +1,78 @@
+"""The calls of the layers around the delta rule from several host threads and streams, and captured in graphs."""
+
+import threading
+
+import pytest
+import torch
+
+import gated_deltanet_chunkwise_gdn_gb300 as gdn
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU runs, skipped there
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+
+def prompt(lengths, D=64, N=16, seed=0):
+    """The arguments of a convolution and of a scan over one packed batch, with pools of their own."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    T, B = sum(lengths), len(lengths)
+    cu = torch.tensor([0] + list(lengths), device="cuda").cumsum(0)
+    idx = torch.randperm(B, generator=gen, device="cuda")
+    x, bc = r(T, D).bfloat16(), r(T, 1, N).bfloat16()
+    conv = (x, r(D, 4), r(D), r(B, 3, D).bfloat16(), idx, cu)
+    scan = (x, x, -torch.rand(D, N, generator=gen, device="cuda"), bc, bc, r(D), x, r(D), r(B, D, N), idx, cu)
+    return conv, scan
+
+
+def outputs(conv, scan, stream=None):
+    """Every call that keeps a workspace, on copies of the pools."""
+    conv, scan = list(conv), list(scan)
+    g = gdn.gdn_conv_backward(*conv, conv[0], stream=stream)
+    conv[3], scan[8] = conv[3].clone(), scan[8].clone()
+    return [gdn.gdn_conv_extend(*conv, stream=stream), conv[3], gdn.gdn_ssm_extend(*scan, stream=stream), scan[8], *g]
+
+
+def in_threads(*jobs):
+    errors = []
+
+    def run(job):
+        try:
+            job()
+        except BaseException as e:  # shown by the test, not by the thread
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+
+
+def test_threads_on_one_stream():
+    """Two threads issue calls of other batches on one stream: each gets its own batch's results."""
+    batches = [prompt([700, 3, 41], seed=1), prompt([5, 1, 9, 0, 260, 2, 30], D=96, seed=2)]
+    want = [outputs(*b) for b in batches]
+    torch.cuda.synchronize()
+
+    def job(i):
+        for _ in range(30):
+            got = outputs(*batches[i])
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+    in_threads(*[lambda i=i: job(i) for i in (0, 1, 0, 1)])
+
+
+def test_two_streams_at_once():
+    batches = [prompt([700, 3, 41], seed=3), prompt([5, 1, 9, 0, 260, 2, 30], D=96, seed=4)]
+    want = [outputs(*b) for b in batches]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    got = []
+    for _ in range(20):
+        for b, s in zip(batches, streams):
+            with torch.cuda.stream(s):
+                got.append(outputs(*b))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))

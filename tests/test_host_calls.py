@@ -1,0 +1,119 @@
+"""What the Python calls do on the host around the library's: workspaces, threads, streams and devices. CPU only: the
+tensors say that they are on a GPU, and the library is a record of the calls made to it."""
+
+import threading
+import time
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+import gated_deltanet_chunkwise_gdn_gb300 as gdn
+from gated_deltanet_chunkwise_gdn_gb300 import _buffers, _lib, mixer
+
+
+class OnGpu(torch.Tensor):
+    """A host tensor that says it is on cuda:0."""
+    device = property(lambda self: torch.device("cuda", 0))
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return 0
+
+
+def on_gpu(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+class Recorder:
+    """Stands in for the library: each call takes a while and is recorded by its workspace's or status word's address."""
+
+    def __init__(self):
+        self.inside, self.overlaps, self.calls, self.lock = {}, 0, [], threading.Lock()
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return lambda *a: 1024
+        if name == "gdn_get_device_status":
+            return lambda word, handle: 0
+
+        def call(*args):
+            key = args[-3] if isinstance(args[-3], int) and args[-3] > 1 << 16 else args[-2]
+            with self.lock:
+                self.overlaps += self.inside.get(key, 0)
+                self.inside[key] = self.inside.get(key, 0) + 1
+                self.calls.append((name, key, args[-1]))
+            time.sleep(0.02)
+            with self.lock:
+                self.inside[key] -= 1
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Recorder()
+    monkeypatch.setattr(_lib, "load", lambda *a: lib)
+    monkeypatch.setattr(_buffers.torch, "empty", lambda n, dtype=None, device=None: torch.zeros(n, dtype=dtype).as_subclass(OnGpu))
+    monkeypatch.setattr(mixer, "_empty", lambda shape, dtype, dev, stream: on_gpu(*shape, dtype=dtype))
+    monkeypatch.setattr(mixer, "_state_grad", lambda pool, n, nb, dev, stream: on_gpu(*pool.shape))
+    for cache in ("_workspaces", "_locks"):
+        monkeypatch.setattr(_buffers, cache, {})
+    return lib
+
+
+STREAM, OTHER = SimpleNamespace(cuda_stream=1 << 20), SimpleNamespace(cuda_stream=2 << 20)
+
+
+def calls():
+    """Every public call, on tensors of one sequence of two tokens."""
+    idx, cu = on_gpu(1, dtype=torch.int64), on_gpu(2, dtype=torch.int64)
+    x, w, pool = on_gpu(2, 8), on_gpu(8, 4), on_gpu(1, 3, 8)
+    A, bc, state = on_gpu(8, 4), on_gpu(2, 1, 4), on_gpu(1, 8, 4)
+    q, a, par, states = on_gpu(2, 1, 64, dtype=torch.bfloat16), on_gpu(2, 1), on_gpu(1), on_gpu(1, 1, 64, 64)
+    out = on_gpu(2, 1, 64, dtype=torch.bfloat16)
+    two, pool2, state2 = on_gpu(2, dtype=torch.int64), on_gpu(2, 3, 8), on_gpu(2, 8, 4)
+    ssm = (x, x, A, bc, bc, None, None, None)
+    return dict(
+        extend=lambda **k: gdn.gdn_extend_chunkwise(q, q, q, a, a, par, par, states, idx, cu, out=out, **k),
+        decode=lambda **k: gdn.gdn_decode_step(q, q, q, a, a, par, par, states, two, out=out, **k),
+        conv_extend=lambda **k: gdn.gdn_conv_extend(x, w, None, pool, idx, cu, **k),
+        conv_step=lambda **k: gdn.gdn_conv_step(x, w, None, pool2, two, **k),
+        conv_backward=lambda **k: gdn.gdn_conv_backward(x, w, None, pool, idx, cu, x, **k),
+        ssm_extend=lambda **k: gdn.gdn_ssm_extend(*ssm, state, idx, cu, **k),
+        ssm_step=lambda **k: gdn.gdn_ssm_step(*ssm, state2, two, **k),
+        ssm_backward=lambda **k: gdn.gdn_ssm_backward(*ssm, state, idx, cu, x, **k),
+        norm=lambda **k: gdn.gdn_layer_norm(x, **k),
+        norm_backward=lambda **k: gdn.gdn_layer_norm_backward(x, x, None, on_gpu(2), on_gpu(2), **k))
+
+
+def in_threads(*jobs):
+    threads = [threading.Thread(target=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+
+
+KEPT = ("extend", "conv_extend", "conv_backward", "ssm_extend")
+
+
+@pytest.mark.parametrize("name", KEPT)
+@pytest.mark.parametrize("other", KEPT)
+def test_threads_on_one_stream_take_turns_on_its_workspace(library, name, other):
+    """A call's kernels are enqueued together: another thread's call on the stream would overwrite what they share."""
+    c = calls()
+    in_threads(*[lambda n=n: c[n](stream=STREAM) for n in (name, other, name)])
+    assert len(library.calls) == 3 and len({key for _, key, _ in library.calls}) == 1
+    assert library.overlaps == 0
+
+
+def test_streams_do_not_wait_for_each_other(library):
+    c = calls()
+    c["conv_extend"](stream=STREAM), c["conv_extend"](stream=OTHER)
+    with _buffers.workspace_lock(torch.device("cuda", 0), STREAM.cuda_stream):
+        t = threading.Thread(target=lambda: c["conv_extend"](stream=OTHER))
+        t.start()
+        t.join(5)
+        assert not t.is_alive()
+    assert len({key for _, key, _ in library.calls}) == 2
