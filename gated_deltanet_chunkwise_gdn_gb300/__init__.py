@@ -19,7 +19,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, kept_workspace, workspace_lock, workspace_of
+from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, kept_workspace, status_word, workspace_lock, workspace_of
 from ._lib import GdnError
 from .mixer import (CausalConv, GdnConvGrads, GdnNormGrads, GdnSsmGrads, LayerNorm, SelectiveScan, gdn_conv_backward,
                     gdn_conv_extend, gdn_conv_step, gdn_layer_norm, gdn_layer_norm_backward, gdn_ssm_backward,
@@ -31,8 +31,6 @@ __all__ = ["gdn_extend_chunkwise", "gdn_decode_step", "gdn_chunkwise_backward", 
            "gdn_conv_extend", "gdn_conv_step", "gdn_conv_backward", "GdnConvGrads", "CausalConv",
            "gdn_ssm_extend", "gdn_ssm_step", "gdn_ssm_backward", "GdnSsmGrads", "SelectiveScan",
            "gdn_layer_norm", "gdn_layer_norm_backward", "GdnNormGrads", "LayerNorm"]
-
-_status_cache: dict = {}
 
 
 def library_path() -> str:
@@ -276,8 +274,8 @@ def gdn_decode_step(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indices, *,
     dedicated kernel: q, k ``[B, H, K]``, v ``[B, HV, V]`` bf16 or fp16; a, b ``[B, HV]``, A_log,
     dt_bias ``[HV]`` fp32; state_pool ``[pool, HV, V, K]`` fp32 (updated in place); cache_indices
     ``[B]`` int64. ``check=True`` waits and raises on a bad or repeated cache index.
-    ``status``: an int32 device tensor for the step's status word; by default one cached word
-    per device, which steps issued concurrently on different streams would share.
+    ``status``: an int32 device tensor for the step's status word, which no step that may run at the same time
+    shares; by default a kept one of the calling thread and stream.
     """
     dev = q.device
     if dev.type != "cuda":
@@ -304,18 +302,15 @@ def gdn_decode_step(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indices, *,
         _req(out, "out", v.dtype, dev)
         if tuple(out.shape) != (B, HV, V):
             raise ValueError("out must be [B, HV, V]")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    sp = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if status is None:
-        status = _status_cache.get(dev.index)
-        if status is None:
-            status = torch.zeros(64, dtype=torch.int32, device=dev)
-            _status_cache[dev.index] = status
+        status = status_word(dev, sp)
     else:
         _req(status, "status", torch.int32, dev)
         if status.numel() < 1:
             raise ValueError("status must hold at least one int32")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    sp = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     L = _lib.load()
     dtype_code = _lib.GDN_BF16 if q.dtype == torch.bfloat16 else _lib.GDN_FP16
     st = L.gdn_decode_step(

@@ -1,4 +1,4 @@
-"""The workspaces that the Python calls keep between them."""
+"""The workspaces and status words that the Python calls keep between them."""
 
 from __future__ import annotations
 
@@ -9,6 +9,7 @@ import torch
 
 _workspaces: dict = {}
 _locks: dict = {}
+_words: dict = {}
 
 UNSHARED = contextlib.nullcontext()  # in the place of a lock, for a workspace that is one call's alone
 
@@ -49,6 +50,19 @@ def workspace_lock(device: torch.device, handle: int):
     key = (device.index, handle)
     lock = _locks.get(key)
     return lock if lock is not None else _locks.setdefault(key, threading.RLock())
+
+
+def status_word(device: torch.device, handle: int) -> torch.Tensor:
+    """The status word of this thread's single-token steps on (device, stream).
+
+    A step may read the word before it writes the pool (its slots' verdict, from a kernel before), so no step
+    that can run, or be enqueued, at the same time may have the same one.
+    """
+    key = (device.index, handle, threading.get_ident())
+    word = _words.get(key)
+    if word is None:
+        word = _words[key] = torch.zeros(64, dtype=torch.int32, device=device)
+    return word
 
 
 def aligned_ptr(buf: torch.Tensor) -> int:

@@ -357,10 +357,12 @@ __global__ void __launch_bounds__(kSsmThreads) ssm_step_any_kernel(SsmParams p, 
   int b, d0;
   split_item((uint64_t)blockIdx.x * (kSsmThreads / 32) + (threadIdx.x >> 5), warps_per_seq, b, d0);
   d0 *= 32;
-  if (!step_slots_ok<CHECK>(p.cache_indices, p.B, p.pool_size, p.status) || b >= p.B) return;
+  const int64_t slot = b < p.B ? p.cache_indices[b] : -1;
+  // A warp stays inside the pool whatever a verdict that came from a kernel before says.
+  if (!step_slots_ok<CHECK>(p.cache_indices, p.B, p.pool_size, p.status) || slot < 0 || slot >= p.pool_size) return;
   const int d = d0 + lane, cells = min(32, p.D - d0) * N;
   const bool has = d < p.D;
-  float* st = p.pool + (p.cache_indices[b] * (int64_t)p.D + d0) * N;
+  float* st = p.pool + (slot * (int64_t)p.D + d0) * N;
   const float* A = p.A + (int64_t)d0 * N;
   const E* Bm = static_cast<const E*>(p.Bm) + b * p.b_stride;
   const E* Cm = static_cast<const E*>(p.Cm) + b * p.c_stride;

@@ -14,12 +14,10 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr, kept_workspace, workspace_lock
+from ._buffers import UNSHARED, aligned_ptr, kept_workspace, status_word, workspace_lock
 from ._lib import GdnError
 
 _DTYPE_CODE = {torch.bfloat16: _lib.GDN_BF16, torch.float16: _lib.GDN_FP16, torch.float32: _lib.GDN_FP32}
-
-_status_cache: dict = {}
 
 
 # ----------------------------------------------------------------------------- arguments
@@ -175,12 +173,10 @@ def _workspace(need, what, workspace, stream, handle, dev, keep):
     return ptr, buf.numel() - (ptr - buf.data_ptr()), buf, lock
 
 
-def _status_word(status, dev):
-    """Address of a step's status word: the caller's, or one cached per device."""
+def _status_word(status, dev, handle):
+    """Address of a step's status word: the caller's, or the one kept for this thread and stream."""
     if status is None:
-        status = _status_cache.get(dev.index)
-        if status is None:
-            status = _status_cache[dev.index] = torch.zeros(64, dtype=torch.int32, device=dev)
+        status = status_word(dev, handle)
     elif not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.device != dev or status.numel() < 1:
         raise ValueError("status must be an int32 tensor on the inputs' device")
     return status.data_ptr()
@@ -256,15 +252,15 @@ def gdn_conv_step(x, weight, bias, conv_pool, cache_indices, *, activation: Opti
                   out: torch.Tensor = None, status: torch.Tensor = None, check: bool = False, stream=None) -> torch.Tensor:
     """:func:`gdn_conv_extend` with one token per sequence: x, out ``[B, D]``.
 
-    ``status``: an int32 device tensor for the step's status word; by default one cached word per device,
-    which steps issued concurrently on different streams would share.
+    ``status``: an int32 device tensor for the step's status word, which no step that may run at the same time
+    shares; by default a kept one of the calling thread and stream.
     """
     dev, dtype, B, D, W, n, _, args, silu = _conv_args(x, weight, bias, conv_pool, cache_indices, activation)
     if n != B:
         raise ValueError("cache_indices must have one entry per sequence")
     stream, handle = _stream(stream, dev)
     out = _out(out, x, dtype, dev, stream)
-    word = _status_word(status, dev)
+    word = _status_word(status, dev, handle)
     st = _lib.load().gdn_conv_step(*args, B, out.data_ptr(), D, W, silu, word, handle)
     _finish(st, "gdn_conv_step", check, word, handle)
     return out
@@ -396,7 +392,7 @@ def gdn_ssm_step(x, dt, A, B, C, D, z, dt_bias, state_pool, cache_indices, *, so
         raise ValueError("cache_indices must have one entry per sequence")
     stream, handle = _stream(stream, dev)
     out = _out(out, x, dtype, dev, stream)
-    word = _status_word(status, dev)
+    word = _status_word(status, dev, handle)
     st = _lib.load().gdn_ssm_step(*args, nb, out.data_ptr(), Dm, G, N, 1 if softplus else 0, word, handle)
     _finish(st, "gdn_ssm_step", check, word, handle)
     return out

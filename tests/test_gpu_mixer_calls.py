@@ -76,3 +76,30 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i, g in enumerate(got):
         assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2]))
+
+
+@pytest.mark.parametrize("N", [16, 5])
+def test_steps_on_two_streams_keep_their_verdicts(N):
+    """A good and a bad batch of steps side by side, both checked by a kernel before: the bad one touches nothing."""
+    B, D = 600, 64
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, bc, A = r(B, D), r(B, 1, N), -torch.rand(D, N, generator=gen, device="cuda")
+    good = torch.randperm(2 * B, generator=gen, device="cuda")[:B]
+    bad = good.clone()
+    bad[B - 1] = bad[0]
+    start = r(2 * B, D, N)
+    pools, streams = [start.clone(), start.clone()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    step = lambda pool, idx: gdn.gdn_ssm_step(x, x, A, bc, bc, None, None, None, pool, idx)  # noqa: E731
+    alone = start.clone()
+    want = [step(alone, good) for _ in range(20)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            got.append(step(pools[0], good))
+        with torch.cuda.stream(streams[1]):
+            step(pools[1], bad)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(pools[0], alone)
+    assert torch.equal(pools[1], start)

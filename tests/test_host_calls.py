@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import gated_deltanet_chunkwise_gdn_gb300 as gdn
-from gated_deltanet_chunkwise_gdn_gb300 import _buffers, _lib, mixer
+from gated_deltanet_chunkwise_gdn_gb300 import _buffers, _lib
 
 
 class OnGpu(torch.Tensor):
@@ -21,8 +21,11 @@ class OnGpu(torch.Tensor):
         return 0
 
 
-def on_gpu(*shape, dtype=torch.float32):
-    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+_zeros = torch.zeros
+
+
+def on_gpu(*shape, dtype=torch.float32, device=None):
+    return _zeros(*shape, dtype=dtype).as_subclass(OnGpu)
 
 
 class Recorder:
@@ -54,10 +57,9 @@ class Recorder:
 def library(monkeypatch):
     lib = Recorder()
     monkeypatch.setattr(_lib, "load", lambda *a: lib)
-    monkeypatch.setattr(_buffers.torch, "empty", lambda n, dtype=None, device=None: torch.zeros(n, dtype=dtype).as_subclass(OnGpu))
-    monkeypatch.setattr(mixer, "_empty", lambda shape, dtype, dev, stream: on_gpu(*shape, dtype=dtype))
-    monkeypatch.setattr(mixer, "_state_grad", lambda pool, n, nb, dev, stream: on_gpu(*pool.shape))
-    for cache in ("_workspaces", "_locks"):
+    for new in ("empty", "zeros"):  # a new tensor "on the GPU"
+        monkeypatch.setattr(torch, new, on_gpu)
+    for cache in ("_workspaces", "_locks", "_words"):
         monkeypatch.setattr(_buffers, cache, {})
     return lib
 
@@ -106,6 +108,27 @@ def test_threads_on_one_stream_take_turns_on_its_workspace(library, name, other)
     in_threads(*[lambda n=n: c[n](stream=STREAM) for n in (name, other, name)])
     assert len(library.calls) == 3 and len({key for _, key, _ in library.calls}) == 1
     assert library.overlaps == 0
+
+
+STEPS = ("decode", "conv_step", "ssm_step")
+
+
+@pytest.mark.parametrize("name", STEPS)
+def test_steps_of_other_streams_and_threads_have_words_of_their_own(library, name):
+    """A step's update may go by the verdict in the status word, so a step beside it must not write there."""
+    step = calls()[name]
+    for stream in (STREAM, STREAM, OTHER, OTHER):
+        step(stream=stream)
+    in_threads(lambda: step(stream=STREAM))
+    words = [key for _, key, _ in library.calls]
+    assert words[0] == words[1] and words[2] == words[3] and len({words[0], words[2], words[4]}) == 3
+
+
+@pytest.mark.parametrize("name", STEPS)
+def test_a_given_status_word_is_used(library, name):
+    word = on_gpu(1, dtype=torch.int32)
+    calls()[name](stream=STREAM, status=word)
+    assert library.calls[0][1] == word.data_ptr()
 
 
 def test_streams_do_not_wait_for_each_other(library):
