@@ -541,6 +541,21 @@ cudaError_t with_row(int vec, int columns, int threads, F&& f) {
   return vec == 2 ? pairs(integral_constant<int, 2>{}) : pairs(integral_constant<int, 1>{});
 }
 
+// The parameters of the longest row that the kernel takes: the limit for all its launches.
+template <typename E, int V>
+constexpr size_t kMostShared = 2 * sizeof(float) * kNormMaxThreads * (V * sizeof(E) == 16 ? kForwardPerThread : kPerThread);
+
+template <typename E, int V, int NV, bool FULL>
+cudaError_t launch_norm_t(const NormParams& p, int threads, cudaStream_t s) {
+  const size_t smem = 2 * align_up((size_t)p.columns * sizeof(float), 16);
+  if (smem > kPlainShared) {
+    static std::atomic<uint64_t> allowed{0};
+    if (cudaError_t e = allow_shared(norm_kernel<E, V, NV, FULL>, kMostShared<E, V>, allowed)) return e;
+  }
+  norm_kernel<E, V, NV, FULL><<<norm_blocks(p.rows, threads), dim3(threads, block_rows(threads)), smem, s>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
@@ -556,15 +571,10 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
       return cudaGetLastError();
     }
     return with_row<E>(vec, p.columns, threads, [&](auto v, auto nv) {
-      const size_t smem = 2 * align_up((size_t)p.columns * sizeof(float), 16);
       constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
-      auto* kernel = norm_kernel<E, V, NV, false>;
       if constexpr (V >= 4)  // (a row of single or paired elements is covered exactly only at an odd address)
-        if (p.columns == threads * NV * V) kernel = norm_kernel<E, V, NV, true>;
-      if (smem > kPlainShared)
-        if (cudaError_t x = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return x;
-      kernel<<<norm_blocks(p.rows, threads), dim3(threads, block_rows(threads)), smem, s>>>(p);
-      return cudaGetLastError();
+        if (p.columns == threads * NV * V) return launch_norm_t<E, V, NV, true>(p, threads, s);
+      return launch_norm_t<E, V, NV, false>(p, threads, s);
     });
   });
 }

@@ -4,6 +4,7 @@
 // packed batch and lays out its work.
 #pragma once
 
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -427,6 +428,20 @@ cudaError_t with_elem(int dtype, F&& f) {
 }
 
 constexpr int kSmCount = 152;  // GB300
+
+// Dynamic shared memory above 48 KB has to be allowed per kernel and device: once, for the largest launch of the
+// kernel, since the limit is the kernel's and a launch of another thread may stand between setting it and using it.
+// `done`: the devices (by their number's low six bits) that have it, one word per kernel.
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) return e;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return cudaSuccess;
+}
 
 // ----------------------------------------------------------------------------- plan of a packed batch
 

@@ -26,8 +26,6 @@
 // shared memory, sums over states take few shuffles (each lane ends up with one channel's sum), and
 // sums over channels are first taken inside the thread and then by one tensor-core product with a
 // matrix of ones: the value split in its upper 11 bits and the rest, both exact to 22 bits in tf32.
-#include <atomic>
-
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -804,18 +802,6 @@ __global__ void __launch_bounds__(32 * kSumRows) ssm_bwd_sum_kernel(SsmParams p,
       if (p.ddt_bias) p.ddt_bias[i - cells - p.D] = a;
     }
   }
-}
-
-// Dynamic shared memory above 48 KB has to be allowed once per kernel and device.
-template <typename K>
-cudaError_t allow_shared(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaError_t e = cudaGetDevice(&dev)) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)) return e;
-  done.fetch_or(bit, std::memory_order_relaxed);
-  return cudaSuccess;
 }
 
 template <typename E, typename M, int VEC>

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import gated_deltanet_chunkwise_gdn_gb300 as gdn
+from gated_deltanet_chunkwise_gdn_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +104,23 @@ def test_steps_on_two_streams_keep_their_verdicts(N):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(pools[0], alone)
     assert torch.equal(pools[1], start)
+
+
+def test_threads_norm_rows_of_several_lengths():
+    """Lengths that run on one kernel with other amounts of shared memory, all above what needs to be allowed. The
+    library is called as closely as the interpreter can, so that calls fall between each other's host steps."""
+    xs = [torch.randn(3, n, device="cuda").bfloat16() for n in (7168, 8192, 12288, 16384)]
+    want = [gdn.gdn_layer_norm(x) for x in xs]
+    outs = [torch.empty_like(x) for x in xs]
+    norm, code = _lib.load().gdn_layer_norm, _lib.GDN_BF16
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+
+    def job(i):
+        x, n = xs[i], xs[i].shape[1]
+        args = (x.data_ptr(), n, code, None, None, outs[i].data_ptr(), None, None, 3, n, 1e-5, streams[i].cuda_stream)
+        status = {norm(*args) for _ in range(20000)}
+        assert status == {0}, status
+    in_threads(*[lambda i=i: job(i) for i in range(len(xs))])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
