@@ -19,7 +19,9 @@ struct NvtxRange {  // host-side range of one call, for timelines
 constexpr int32_t kMaxStepBatch = 1 << 20;
 constexpr int64_t kMaxBlocks = INT32_MAX;
 
-bool batch_sizes_ok(int64_t T, int32_t B) { return T >= 0 && T < (int64_t)INT32_MAX && B >= 0; }
+// The kernels count a segment's tokens in 32 bits, up to a tile (64 tokens) past its end.
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1024;
+bool batch_sizes_ok(int64_t T, int32_t B) { return T >= 0 && T <= kMaxTokens && B >= 0; }
 
 bool stride_ok(int64_t stride, int64_t row) { return stride >= row && stride < ((int64_t)1 << 40); }
 

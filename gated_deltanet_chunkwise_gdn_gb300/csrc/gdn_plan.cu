@@ -9,7 +9,8 @@ namespace {
 
 constexpr int kPlanThreads = 1024;  // and the largest batch that is checked and laid out in shared memory
 
-__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// (a >= 0; a + b may not fit in 32 bits)
+__device__ __forceinline__ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
 // Sum over the warp's lanes, in every lane.
 __device__ __forceinline__ int warp_sum_int(int x) { return __reduce_add_sync(0xffffffffu, x); }

@@ -262,8 +262,8 @@ GDN_API gdn_status gdn_chunkwise_backward(const void *q, const void *k, const vo
  * Common rules. Activations are bf16, fp16 or fp32 (one dtype a call), parameters fp32, sums and
  * states of the scan fp32. An activation given with a row stride (in elements, at least the row's
  * length) may be a column slice of a wider array; its rows are dense. Arrays without a stride are
- * dense. Pointers are aligned to their elements; 16-byte aligned rows and channel counts run on the
- * wide loads. Packed batches, slots, streams and errors are as for gdn_extend_chunkwise above: bad
+ * dense. total_tokens is at most 2^31 - 1024. Pointers are aligned to their elements; 16-byte aligned
+ * rows and channel counts run on the wide loads. Packed batches, slots, streams and errors are as for gdn_extend_chunkwise above: bad
  * cu_seqlens or cache_indices are found on the device, the call's later kernels then do nothing, and
  * the status is read with gdn_get_device_status from the workspace (or the step's status word).
  * Sums over tokens, rows or channels are taken in a fixed order: equal calls give equal bits.
