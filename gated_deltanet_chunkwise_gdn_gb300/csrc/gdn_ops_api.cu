@@ -23,6 +23,9 @@ constexpr int64_t kMaxBlocks = INT32_MAX;
 constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 1024;
 bool batch_sizes_ok(int64_t T, int32_t B) { return T >= 0 && T <= kMaxTokens && B >= 0; }
 
+// The kernels count a row's columns in 32 bits, up to a block's share of them past its end.
+constexpr int32_t kMaxColumns = 1 << 30;
+
 bool stride_ok(int64_t stride, int64_t row) { return stride >= row && stride < ((int64_t)1 << 40); }
 
 bool workspace_ok(const void* ws, size_t have, size_t need) { return ws && have >= need && aligned_to(ws, 256); }
@@ -456,10 +459,11 @@ gdn_status gdn_layer_norm(const void* x, int64_t x_stride, gdn_dtype dtype, cons
   if (rows < 0 || columns <= 0 || !(eps >= 0.f) || !gdn::op_dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
   const uintptr_t size = gdn::op_dtype_size(dtype);
   if (!aligned_to(weight, 4) || !aligned_to(bias, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)) return GDN_ERR_INVALID_ARG;
-  if (rows == 0) return GDN_OK;
-  if (!x || !out || !aligned_to(x, size) || !aligned_to(out, size) || !stride_ok(x_stride, columns) ||
-      (mean == nullptr) != (rstd == nullptr))
+  if (rows > 0 && (!x || !out || !aligned_to(x, size) || !aligned_to(out, size) || !stride_ok(x_stride, columns) ||
+                   (mean == nullptr) != (rstd == nullptr)))
     return GDN_ERR_INVALID_ARG;
+  if (columns > kMaxColumns) return GDN_ERR_UNSUPPORTED;
+  if (rows == 0) return GDN_OK;
   gdn::NormParams p{};
   p.x = x;
   p.weight = weight;
@@ -476,7 +480,7 @@ gdn_status gdn_layer_norm(const void* x, int64_t x_stride, gdn_dtype dtype, cons
 }
 
 size_t gdn_layer_norm_backward_workspace_size(int64_t rows, int32_t columns) {
-  return rows < 0 || columns <= 0 ? 0 : gdn::norm_backward_workspace(rows, columns);
+  return rows < 0 || columns <= 0 || columns > kMaxColumns ? 0 : gdn::norm_backward_workspace(rows, columns);
 }
 
 gdn_status gdn_layer_norm_backward(const void* d_out, int64_t d_out_stride, const void* x, int64_t x_stride, gdn_dtype dtype,
@@ -491,6 +495,7 @@ gdn_status gdn_layer_norm_backward(const void* d_out, int64_t d_out_stride, cons
                    !aligned_to(dx, size) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !stride_ok(x_stride, columns) ||
                    !stride_ok(d_out_stride, columns)))
     return GDN_ERR_INVALID_ARG;
+  if (columns > kMaxColumns) return GDN_ERR_UNSUPPORTED;
   if (!workspace_ok(workspace, workspace_bytes, gdn::norm_backward_workspace(rows, columns))) return GDN_ERR_WORKSPACE;
   gdn::NormParams p{};
   p.x = x;

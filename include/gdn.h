@@ -396,7 +396,8 @@ GDN_API gdn_status gdn_ssm_backward(const void *x, int64_t x_stride, const void 
  *  weight, bias  [columns] fp32 or NULL (1 and 0).
  *  mean, rstd    [rows] fp32, written; both or neither NULL.
  *  eps           >= 0.
- *  rows >= 0, columns >= 1. Each row is computed by itself, in an order that its length alone fixes.
+ *  rows >= 0, 1 <= columns <= 2^30 (above: GDN_ERR_UNSUPPORTED). Each row is computed by itself, in an order
+ *  that its length alone fixes.
  */
 GDN_API gdn_status gdn_layer_norm(const void *x, int64_t x_stride, gdn_dtype dtype, const float *weight,
                                   const float *bias, void *out, float *mean, float *rstd, int64_t rows,

@@ -31,3 +31,16 @@ def test_most_tokens_of_one_channel(B):
     gdn.gdn_ssm_extend(x, one, torch.full((1, 1), -200.0, device="cuda"), one[:, None], one[:, None], None, None, None, state, idx,
                        cu, softplus=False, out=out, check=True)
     assert torch.equal(out, x) and torch.equal(state[idx, 0], x[cu[1:] - 1].float())
+
+
+def test_longest_row_of_layer_norm():
+    """2^30 columns of one value but for two: the mean, the variance and the gradients follow by hand."""
+    n = 1 << 30
+    x = torch.full((1, n), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[0, 5], x[0, n - 1] = 4.0, 0.0                    # mean 2, variance 8 / n
+    out, mean, rstd = gdn.gdn_layer_norm(x, eps=1.0, return_stats=True)
+    assert float(mean) == 2.0 and float(rstd) == 1.0   # (8 / n is under half a step of 1)
+    assert float(out[0, 5]) == 2.0 and float(out[0, n - 1]) == -2.0 and int((out == 0).sum()) == n - 2
+    g = gdn.gdn_layer_norm_backward(out, x, None, mean, rstd)  # the output as its own gradient: mean 0, mean of dy xh 8 / n
+    assert torch.equal(g.dx, out) and torch.equal(g.dbias, out[0].float())
+    assert float(g.dweight[5]) == 4.0 and float(g.dweight[n - 1]) == 4.0 and int((g.dweight == 0).sum()) == n - 2
