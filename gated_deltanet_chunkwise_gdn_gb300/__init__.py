@@ -19,7 +19,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, kept_workspace, status_word, workspace_lock, workspace_of
+from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, status_word, workspace_for, workspace_of
 from ._lib import GdnError
 from .mixer import (CausalConv, GdnConvGrads, GdnNormGrads, GdnSsmGrads, LayerNorm, SelectiveScan, gdn_conv_backward,
                     gdn_conv_extend, gdn_conv_step, gdn_layer_norm, gdn_layer_norm_backward, gdn_ssm_backward,
@@ -65,7 +65,9 @@ def gdn_extend_chunkwise(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indice
     A_log, dt_bias ``[HV]`` fp32; state_pool ``[pool, HV, V, K]`` fp32 (updated in
     place); cache_indices ``[B]`` and cu_seqlens ``[B+1]`` int64 on the same device.
     ``check=True`` waits for the device and raises on a device-detected error
-    (bad cache index or cu_seqlens).
+    (bad cache index or cu_seqlens). ``workspace``: memory for the call's intermediates (256-byte aligned, at least
+    :func:`gdn_workspace_size` bytes, its first int32 the call's status); by default a kept one of the stream, or
+    the graph's own in a capture.
     """
     dev = q.device
     if dev.type != "cuda":
@@ -99,16 +101,13 @@ def gdn_extend_chunkwise(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indice
     need = int(L.gdn_workspace_size(T, B, H, HV, K, V, chunk_size))
     if need == 0:
         raise GdnError(2, f"unsupported sizes (K={K}, V={V}, chunk_size={chunk_size}, H={H}, HV={HV})")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif not hasattr(stream, "cuda_stream"):
+    if stream is not None and not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    sp = stream.cuda_stream
+    sp = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
     lock = UNSHARED
     if workspace is None:
-        ws = kept_workspace(dev, stream, need)
+        ws, lock = workspace_for(dev, stream, sp, need)
         ws_ptr, ws_bytes = _aligned_ptr(ws), ws.numel() - (_aligned_ptr(ws) - ws.data_ptr())
-        lock = workspace_lock(dev, sp)
     else:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     dtype_code = _lib.GDN_BF16 if q.dtype == torch.bfloat16 else _lib.GDN_FP16
@@ -275,7 +274,7 @@ def gdn_decode_step(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indices, *,
     dt_bias ``[HV]`` fp32; state_pool ``[pool, HV, V, K]`` fp32 (updated in place); cache_indices
     ``[B]`` int64. ``check=True`` waits and raises on a bad or repeated cache index.
     ``status``: an int32 device tensor for the step's status word, which no step that may run at the same time
-    shares; by default a kept one of the calling thread and stream.
+    shares; by default a kept one of the calling thread and stream, or the graph's own in a capture.
     """
     dev = q.device
     if dev.type != "cuda":
@@ -302,11 +301,11 @@ def gdn_decode_step(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indices, *,
         _req(out, "out", v.dtype, dev)
         if tuple(out.shape) != (B, HV, V):
             raise ValueError("out must be [B, HV, V]")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    sp = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    sp = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
     if status is None:
-        status = status_word(dev, sp)
+        status = status_word(dev, stream, sp)
     else:
         _req(status, "status", torch.int32, dev)
         if status.numel() < 1:

@@ -14,24 +14,45 @@ _words: dict = {}
 UNSHARED = contextlib.nullcontext()  # in the place of a lock, for a workspace that is one call's alone
 
 
-def kept_workspace(device: torch.device, stream: torch.cuda.Stream, nbytes: int) -> torch.Tensor:
-    """The kept workspace of (device, stream), with room for `nbytes` at a 256-byte boundary.
+def _capturing(stream) -> bool:
+    """Whether a graph is being captured on the stream (None: the current one)."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
 
-    One buffer per stream: calls on one stream are ordered, so they may share it, while calls
+
+def _new(n: int, dtype, device: torch.device, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(n, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=dtype, device=device)
+
+
+def workspace_for(device: torch.device, stream, handle: int, nbytes: int):
+    """(workspace, lock to hold while the call is enqueued) of a call on the stream (None: the current one) of this
+    handle, with room for `nbytes` at a 256-byte boundary.
+
+    One kept buffer per stream: calls on one stream are ordered, so they may share it, while calls
     on two streams of a device run concurrently and must not. The buffer is allocated on the
     call's stream, so when it is replaced by a larger one, the caching allocator reuses the old
     memory only in that stream's order, after the calls already enqueued there.
+
+    A call that is captured into a graph gets a buffer of its own instead, from the graph's memory: the graph may be
+    replayed on any stream, beside calls on the stream that it was captured on and beside other graphs
+    captured there, and after a larger call has replaced the kept buffer.
     """
-    key = (device.index, stream.cuda_stream)
+    if _capturing(stream):
+        return _new(nbytes + 256, torch.uint8, device, stream), UNSHARED
+    key = (device.index, handle)
+    lock = workspace_lock(device, handle)
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes + 256:
-        with workspace_lock(device, stream.cuda_stream):
+        with lock:
             buf = _workspaces.get(key)
             if buf is None or buf.numel() < nbytes + 256:
-                with torch.cuda.stream(stream):
-                    buf = torch.empty(max(nbytes, 256) + 256, dtype=torch.uint8, device=device)
-                _workspaces[key] = buf
-    return buf
+                buf = _workspaces[key] = _new(max(nbytes, 256) + 256, torch.uint8, device, stream)
+    return buf, lock
 
 
 def workspace_of(device_index, handle: int):
@@ -52,16 +73,19 @@ def workspace_lock(device: torch.device, handle: int):
     return lock if lock is not None else _locks.setdefault(key, threading.RLock())
 
 
-def status_word(device: torch.device, handle: int) -> torch.Tensor:
-    """The status word of this thread's single-token steps on (device, stream).
+def status_word(device: torch.device, stream, handle: int) -> torch.Tensor:
+    """The status word of this thread's single-token steps on the stream (None: the current one) of this handle.
 
     A step may read the word before it writes the pool (its slots' verdict, from a kernel before), so no step
-    that can run, or be enqueued, at the same time may have the same one.
+    that can run, or be enqueued, at the same time may have the same one; a step that is captured into a graph
+    has one of the graph's own, as a workspace would be. Every step writes the word before it reads it.
     """
+    if _capturing(stream):
+        return _new(1, torch.int32, device, stream)
     key = (device.index, handle, threading.get_ident())
     word = _words.get(key)
     if word is None:
-        word = _words[key] = torch.zeros(64, dtype=torch.int32, device=device)
+        word = _words[key] = _new(1, torch.int32, device, stream)
     return word
 
 

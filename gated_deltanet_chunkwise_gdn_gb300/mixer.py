@@ -14,7 +14,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr, kept_workspace, status_word, workspace_lock
+from ._buffers import UNSHARED, aligned_ptr, status_word, workspace_for
 from ._lib import GdnError
 
 _DTYPE_CODE = {torch.bfloat16: _lib.GDN_BF16, torch.float16: _lib.GDN_FP16, torch.float32: _lib.GDN_FP32}
@@ -165,21 +165,20 @@ def _workspace(need, what, workspace, stream, handle, dev, keep):
     if workspace is not None:
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace, UNSHARED
     if keep:
-        buf = kept_workspace(dev, torch.cuda.current_stream(dev) if stream is None else stream, need)
-        lock = workspace_lock(dev, handle)
+        buf, lock = workspace_for(dev, stream, handle, need)
     else:
         buf, lock = _empty((need + 256,), torch.uint8, dev, stream), UNSHARED
     ptr = aligned_ptr(buf)
     return ptr, buf.numel() - (ptr - buf.data_ptr()), buf, lock
 
 
-def _status_word(status, dev, handle):
-    """Address of a step's status word: the caller's, or the one kept for this thread and stream."""
+def _status_word(status, dev, stream, handle):
+    """(a step's status word, its address): the caller's, or the one kept for this thread and stream."""
     if status is None:
-        status = status_word(dev, handle)
+        status = status_word(dev, stream, handle)
     elif not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.device != dev or status.numel() < 1:
         raise ValueError("status must be an int32 tensor on the inputs' device")
-    return status.data_ptr()
+    return status, status.data_ptr()
 
 
 def _finish(st, what, check, word, handle):
@@ -233,7 +232,9 @@ def gdn_conv_extend(x, weight, bias, conv_pool, cache_indices, cu_seqlens, *, ac
     x ``[T, D]``; weight ``[D, W]`` fp32 with W = 2, 3 or 4 (the last tap meets the newest token); bias
     ``[D]`` fp32 or None; conv_pool ``[pool, W - 1, D]`` in x's dtype, each slot's last W - 1 inputs, oldest
     first, updated in place; cache_indices ``[B]``, cu_seqlens ``[B + 1]`` int64. ``activation`` is
-    ``"silu"`` or None. ``check=True`` waits and raises on a bad slot or bad cu_seqlens.
+    ``"silu"`` or None. ``check=True`` waits and raises on a bad slot or bad cu_seqlens. ``workspace``: memory for the
+    call's plan (256-byte aligned; its first int32 becomes the call's status); by default a kept one of the stream,
+    or the graph's own in a capture.
     """
     dev, dtype, T, D, W, B, pool, args, silu = _conv_args(x, weight, bias, conv_pool, cache_indices, activation)
     cp = _dense(cu_seqlens, "cu_seqlens", torch.int64, dev, (B + 1,))
@@ -253,14 +254,14 @@ def gdn_conv_step(x, weight, bias, conv_pool, cache_indices, *, activation: Opti
     """:func:`gdn_conv_extend` with one token per sequence: x, out ``[B, D]``.
 
     ``status``: an int32 device tensor for the step's status word, which no step that may run at the same time
-    shares; by default a kept one of the calling thread and stream.
+    shares; by default a kept one of the calling thread and stream, or the graph's own in a capture.
     """
     dev, dtype, B, D, W, n, _, args, silu = _conv_args(x, weight, bias, conv_pool, cache_indices, activation)
     if n != B:
         raise ValueError("cache_indices must have one entry per sequence")
     stream, handle = _stream(stream, dev)
     out = _out(out, x, dtype, dev, stream)
-    word = _status_word(status, dev, handle)
+    _keep, word = _status_word(status, dev, stream, handle)
     st = _lib.load().gdn_conv_step(*args, B, out.data_ptr(), D, W, silu, word, handle)
     _finish(st, "gdn_conv_step", check, word, handle)
     return out
@@ -392,7 +393,7 @@ def gdn_ssm_step(x, dt, A, B, C, D, z, dt_bias, state_pool, cache_indices, *, so
         raise ValueError("cache_indices must have one entry per sequence")
     stream, handle = _stream(stream, dev)
     out = _out(out, x, dtype, dev, stream)
-    word = _status_word(status, dev, handle)
+    _keep, word = _status_word(status, dev, stream, handle)
     st = _lib.load().gdn_ssm_step(*args, nb, out.data_ptr(), Dm, G, N, 1 if softplus else 0, word, handle)
     _finish(st, "gdn_ssm_step", check, word, handle)
     return out

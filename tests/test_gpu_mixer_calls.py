@@ -124,3 +124,54 @@ def test_threads_norm_rows_of_several_lengths():
     in_threads(*[lambda i=i: job(i) for i in range(len(xs))])
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_graphs_beside_calls_on_their_stream():
+    """Two graphs captured on one stream after its workspace is made, replayed side by side on others, with larger calls
+    on that stream in between, whose workspace replaces the one before."""
+    batches = [prompt([300, 7, 41], seed=6), prompt([5, 1, 9, 0, 260, 2, 30], D=96, seed=7)]
+    large = prompt([9000] + [5] * 700, seed=8)
+    want = [outputs(*b) for b in batches]
+    want_large = outputs(*large)
+    main = torch.cuda.Stream()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        outputs(*batches[0])
+    main.synchronize()
+    graphs, results = [], []
+    for b in batches:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=main):
+            results.append(outputs(*b))
+    for _ in range(10):
+        for t in [t for r in results for t in r]:
+            t.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(main):
+            got = outputs(*large)
+            spare = [torch.full((1 << 18,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        torch.cuda.synchronize()
+        for r, w in zip(results + [got], want + [want_large]):
+            assert all(torch.equal(a, b) for a, b in zip(r, w))
+        assert all(bool((t == 7).all()) for t in spare)
+
+
+def test_a_replayed_step_reports_to_a_given_word():
+    B, D = 400, 64
+    x, w, pool = torch.randn(B, D, device="cuda"), torch.randn(D, 4, device="cuda"), torch.randn(B, 3, D, device="cuda")
+    idx, word = torch.arange(B, device="cuda"), torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    gdn.gdn_conv_step(x, w, None, pool.clone(), idx)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.gdn_conv_step(x, w, None, pool, idx, status=word)
+    graph.replay()
+    assert int(word) == 0
+    before = pool.clone()
+    idx[3] = idx[2]
+    graph.replay()
+    assert int(word) == 3 and torch.equal(pool, before)

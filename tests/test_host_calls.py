@@ -59,6 +59,8 @@ def library(monkeypatch):
     monkeypatch.setattr(_lib, "load", lambda *a: lib)
     for new in ("empty", "zeros"):  # a new tensor "on the GPU"
         monkeypatch.setattr(torch, new, on_gpu)
+    lib.capturing = False
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: lib.capturing)
     for cache in ("_workspaces", "_locks", "_words"):
         monkeypatch.setattr(_buffers, cache, {})
     return lib
@@ -140,3 +142,25 @@ def test_streams_do_not_wait_for_each_other(library):
         t.join(5)
         assert not t.is_alive()
     assert len({key for _, key, _ in library.calls}) == 2
+
+
+@pytest.mark.parametrize("name", KEPT + STEPS)
+def test_captured_calls_have_buffers_of_their_own(library, name):
+    """A graph is replayed beside calls on the stream it was captured on, and after their buffer has grown."""
+    call, kept = calls()[name], []
+    call(stream=STREAM)
+    library.capturing = True
+    empty = torch.empty
+
+    def keep(*a, **k):  # so that no two of them can have the same address by turns
+        kept.append(empty(*a, **k))
+        return kept[-1]
+    torch.empty = keep
+    try:
+        call(stream=STREAM), call(stream=STREAM)
+    finally:
+        torch.empty = empty
+    library.capturing = False
+    call(stream=STREAM)
+    at = [key for _, key, _ in library.calls]
+    assert at[0] == at[3] and len(set(at)) == 3
