@@ -19,7 +19,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, status_word, workspace_for, workspace_of
+from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, given_workspace, status_word, workspace_for, workspace_of
 from ._lib import GdnError
 from .mixer import (CausalConv, GdnConvGrads, GdnNormGrads, GdnSsmGrads, LayerNorm, SelectiveScan, gdn_conv_backward,
                     gdn_conv_extend, gdn_conv_step, gdn_layer_norm, gdn_layer_norm_backward, gdn_ssm_backward,
@@ -109,7 +109,7 @@ def gdn_extend_chunkwise(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indice
         ws, lock = workspace_for(dev, stream, sp, need)
         ws_ptr, ws_bytes = _aligned_ptr(ws), ws.numel() - (_aligned_ptr(ws) - ws.data_ptr())
     else:
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = given_workspace(workspace, dev)
     dtype_code = _lib.GDN_BF16 if q.dtype == torch.bfloat16 else _lib.GDN_FP16
     with lock:
         st = L.gdn_extend_chunkwise(
@@ -215,7 +215,7 @@ def gdn_chunkwise_backward(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indi
             ws_ptr = _aligned_ptr(ws)
             ws_bytes = ws.numel() - (ws_ptr - ws.data_ptr())
         else:
-            ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            ws_ptr, ws_bytes = given_workspace(workspace, dev)
     dtype_code = _lib.GDN_BF16 if q.dtype == torch.bfloat16 else _lib.GDN_FP16
     st = L.gdn_chunkwise_backward(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype_code,

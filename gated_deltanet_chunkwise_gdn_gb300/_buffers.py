@@ -55,6 +55,17 @@ def workspace_for(device: torch.device, stream, handle: int, nbytes: int):
     return buf, lock
 
 
+def given_workspace(workspace, device: torch.device):
+    """(address, bytes) of a caller's workspace."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def workspace_of(device_index, handle: int):
     """The kept workspace of (device, stream) or None."""
     return _workspaces.get((device_index, handle))

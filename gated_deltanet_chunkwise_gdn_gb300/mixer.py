@@ -14,7 +14,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr, status_word, workspace_for
+from ._buffers import UNSHARED, aligned_ptr, given_workspace, status_word, workspace_for
 from ._lib import GdnError
 
 _DTYPE_CODE = {torch.bfloat16: _lib.GDN_BF16, torch.float16: _lib.GDN_FP16, torch.float32: _lib.GDN_FP32}
@@ -163,7 +163,7 @@ def _workspace(need, what, workspace, stream, handle, dev, keep):
     if need == 0:
         raise GdnError(2, f"{what}: unsupported sizes")
     if workspace is not None:
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace, UNSHARED
+        return *given_workspace(workspace, dev), workspace, UNSHARED
     if keep:
         buf, lock = workspace_for(dev, stream, handle, need)
     else:

@@ -41,7 +41,7 @@ class Recorder:
             return lambda word, handle: 0
 
         def call(*args):
-            key = args[-3] if isinstance(args[-3], int) and args[-3] > 1 << 16 else args[-2]
+            key = args[-3] if args[-3] and args[-3] > 1 << 16 else args[-2]
             with self.lock:
                 self.overlaps += self.inside.get(key, 0)
                 self.inside[key] = self.inside.get(key, 0) + 1
@@ -60,6 +60,7 @@ def library(monkeypatch):
     for new in ("empty", "zeros"):  # a new tensor "on the GPU"
         monkeypatch.setattr(torch, new, on_gpu)
     lib.capturing = False
+    monkeypatch.setattr(torch, "zeros_like", lambda t: on_gpu(*t.shape, dtype=t.dtype))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: lib.capturing)
     for cache in ("_workspaces", "_locks", "_words"):
         monkeypatch.setattr(_buffers, cache, {})
@@ -80,6 +81,7 @@ def calls():
     ssm = (x, x, A, bc, bc, None, None, None)
     return dict(
         extend=lambda **k: gdn.gdn_extend_chunkwise(q, q, q, a, a, par, par, states, idx, cu, out=out, **k),
+        backward=lambda **k: gdn.gdn_chunkwise_backward(q, q, q, a, a, par, par, states, idx, cu, q, **k),
         decode=lambda **k: gdn.gdn_decode_step(q, q, q, a, a, par, par, states, two, out=out, **k),
         conv_extend=lambda **k: gdn.gdn_conv_extend(x, w, None, pool, idx, cu, **k),
         conv_step=lambda **k: gdn.gdn_conv_step(x, w, None, pool2, two, **k),
@@ -164,3 +166,16 @@ def test_captured_calls_have_buffers_of_their_own(library, name):
     call(stream=STREAM)
     at = [key for _, key, _ in library.calls]
     assert at[0] == at[3] and len(set(at)) == 3
+
+
+@pytest.mark.parametrize("name", KEPT + ("ssm_backward", "norm_backward", "backward"))
+def test_a_workspace_elsewhere_is_refused(library, name):
+    """The kernels write there: host memory, gaps and other objects never reach the library."""
+    call = calls()[name]
+    room = on_gpu(8192, dtype=torch.uint8)
+    for bad, error in ((_zeros(8192, dtype=torch.uint8), ValueError), (room[::2], ValueError), (room.data_ptr(), TypeError)):
+        with pytest.raises(error, match="workspace"):
+            call(stream=STREAM, workspace=bad)
+    assert not library.calls
+    call(stream=STREAM, workspace=room)
+    assert library.calls[0][1] == room.data_ptr()
