@@ -19,7 +19,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, given_workspace, status_word, workspace_for, workspace_of
+from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, given_workspace, require_current, status_word, workspace_for, workspace_of
 from ._lib import GdnError
 from .mixer import (CausalConv, GdnConvGrads, GdnNormGrads, GdnSsmGrads, LayerNorm, SelectiveScan, gdn_conv_backward,
                     gdn_conv_extend, gdn_conv_step, gdn_layer_norm, gdn_layer_norm_backward, gdn_ssm_backward,
@@ -72,6 +72,7 @@ def gdn_extend_chunkwise(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indice
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("gdn_extend_chunkwise runs on a CUDA device; move the inputs there first")
+    require_current(dev)
     act = (torch.bfloat16, torch.float16)
     _req(q, "q", act, dev)
     _req(k, "k", q.dtype, dev)
@@ -159,6 +160,7 @@ def gdn_chunkwise_backward(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indi
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("gdn_chunkwise_backward runs on a CUDA device; move the inputs there first")
+    require_current(dev)
     _req(q, "q", (torch.bfloat16, torch.float16), dev)
     _req(k, "k", q.dtype, dev)
     _req(v, "v", q.dtype, dev)
@@ -279,6 +281,7 @@ def gdn_decode_step(q, k, v, a, b, A_log, dt_bias, state_pool, cache_indices, *,
     dev = q.device
     if dev.type != "cuda":
         raise ValueError("gdn_decode_step runs on a CUDA device; move the inputs there first")
+    require_current(dev)
     _req(q, "q", (torch.bfloat16, torch.float16), dev)
     _req(k, "k", q.dtype, dev)
     _req(v, "v", q.dtype, dev)

@@ -14,6 +14,16 @@ _words: dict = {}
 UNSHARED = contextlib.nullcontext()  # in the place of a lock, for a workspace that is one call's alone
 
 
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def require_current(device: torch.device) -> None:
+    """The library launches on the thread's current device: the inputs' has to be that one."""
+    if _device() != device.index:
+        raise ValueError(f"the inputs are on {device}, but the current device is cuda:{_device()}: make the call under "
+                         f"torch.cuda.device({device.index})")
+
+
 def _capturing(stream) -> bool:
     """Whether a graph is being captured on the stream (None: the current one)."""
     if stream is None:

@@ -60,6 +60,8 @@ def library(monkeypatch):
     for new in ("empty", "zeros"):  # a new tensor "on the GPU"
         monkeypatch.setattr(torch, new, on_gpu)
     lib.capturing = False
+    lib.device = 0
+    monkeypatch.setattr(_buffers, "_device", lambda: lib.device)
     monkeypatch.setattr(torch, "zeros_like", lambda t: on_gpu(*t.shape, dtype=t.dtype))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: lib.capturing)
     for cache in ("_workspaces", "_locks", "_words"):
@@ -179,3 +181,16 @@ def test_a_workspace_elsewhere_is_refused(library, name):
     assert not library.calls
     call(stream=STREAM, workspace=room)
     assert library.calls[0][1] == room.data_ptr()
+
+
+@pytest.mark.parametrize("name", ["extend", "backward", "decode", "conv_extend", "conv_step", "conv_backward", "ssm_extend", "ssm_step",
+                                  "ssm_backward", "norm", "norm_backward"])
+def test_inputs_off_the_current_device_are_refused(library, name):
+    """The kernels would run on the current device with the other one's addresses."""
+    library.device = 1
+    with pytest.raises(ValueError, match="current device is cuda:1"):
+        calls()[name](stream=STREAM)
+    assert not library.calls
+    library.device = 0
+    calls()[name](stream=STREAM)
+    assert len(library.calls) == 1
