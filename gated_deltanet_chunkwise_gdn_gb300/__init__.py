@@ -17,6 +17,7 @@ from __future__ import annotations
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._buffers import UNSHARED, aligned_ptr as _aligned_ptr, given_workspace, require_current, status_word, workspace_for, workspace_of
@@ -240,7 +241,7 @@ class GatedDeltaNetChunkwise(torch.autograd.Function):
     ``apply(q, k, v, a, b, A_log, dt_bias, initial_state, cu_seqlens, chunk_size=64, scale=1.0)`` with
     ``initial_state [B, HV, V, K]`` fp32 (one state per sequence) returns ``(out [T, HV, V],
     final_state [B, HV, V, K])``; gradients flow to q, k, v, a, b, A_log, dt_bias and initial_state
-    (q, k, v get their gradients in their own dtype, the rest in fp32).
+    (q, k, v get their gradients in their own dtype, the rest in fp32). Second derivatives are an error.
     """
 
     @staticmethod
@@ -254,6 +255,7 @@ class GatedDeltaNetChunkwise(torch.autograd.Function):
         return out, pool
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_final):
         q, k, v, a, b, A_log, dt_bias, initial_state, cu_seqlens, idx = ctx.saved_tensors
         if d_out is None:

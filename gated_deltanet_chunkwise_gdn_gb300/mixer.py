@@ -12,6 +12,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._buffers import UNSHARED, aligned_ptr, given_workspace, require_current, status_word, workspace_for
@@ -520,6 +521,9 @@ def gdn_layer_norm_backward(d_out, x, weight, mean, rstd, *, workspace: torch.Te
 # ----------------------------------------------------------------------------- autograd
 
 
+# (The backward passes are kernels without gradients of their own: once_differentiable makes a second derivative an
+# error, where it would otherwise be zero in silence.)
+
 def _own_slots(state, x):
     return torch.arange(state.shape[0], dtype=torch.int64, device=x.device)
 
@@ -527,7 +531,7 @@ def _own_slots(state, x):
 class CausalConv(torch.autograd.Function):
     """The convolution as an autograd function: ``apply(x, weight, bias, initial_state, cu_seqlens,
     activation="silu")`` with ``initial_state [B, W - 1, D]`` in x's dtype (one per sequence) returns
-    ``(out, final_state)``; gradients flow to x, weight, bias and initial_state."""
+    ``(out, final_state)``; gradients flow to x, weight, bias and initial_state. Second derivatives are an error."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, initial_state, cu_seqlens, activation="silu"):
@@ -538,6 +542,7 @@ class CausalConv(torch.autograd.Function):
         return out, pool
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_final):
         x, weight, bias, state, cu = ctx.saved_tensors
         d_out = torch.zeros_like(x, memory_format=torch.contiguous_format) if d_out is None else d_out.to(x.dtype).contiguous()
@@ -550,7 +555,7 @@ class CausalConv(torch.autograd.Function):
 class SelectiveScan(torch.autograd.Function):
     """The scan as an autograd function: ``apply(x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens,
     softplus=True)`` with ``initial_state [B, Dm, N]`` fp32 (one per sequence) returns ``(out,
-    final_state)``; gradients flow to every tensor but cu_seqlens."""
+    final_state)``; gradients flow to every tensor but cu_seqlens. Second derivatives are an error."""
 
     @staticmethod
     def forward(ctx, x, dt, A, B, C, D, z, dt_bias, initial_state, cu_seqlens, softplus=True):
@@ -561,6 +566,7 @@ class SelectiveScan(torch.autograd.Function):
         return out, pool
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_final):
         x, dt, A, B, C, D, z, dt_bias, state, cu = ctx.saved_tensors
         d_out = torch.zeros_like(x, memory_format=torch.contiguous_format) if d_out is None else d_out.to(x.dtype).contiguous()
@@ -572,7 +578,7 @@ class SelectiveScan(torch.autograd.Function):
 
 class LayerNorm(torch.autograd.Function):
     """Layer norm as an autograd function: ``apply(x, weight, bias, eps=1e-5)``; gradients flow to x, weight
-    and bias."""
+    and bias. Second derivatives are an error."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, eps=1e-5):
@@ -582,6 +588,7 @@ class LayerNorm(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out):
         x, weight, mean, rstd = ctx.saved_tensors
         g = gdn_layer_norm_backward(d_out.to(x.dtype).contiguous(), x, weight, mean, rstd)

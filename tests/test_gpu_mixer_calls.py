@@ -175,3 +175,11 @@ def test_a_replayed_step_reports_to_a_given_word():
     idx[3] = idx[2]
     graph.replay()
     assert int(word) == 3 and torch.equal(pool, before)
+
+
+def test_a_gradient_penalty_is_refused():
+    x = torch.randn(5, 64, device="cuda", requires_grad=True)
+    out = gdn.LayerNorm.apply(x, None, None)
+    g, = torch.autograd.grad(out.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (out.sum() + g.square().sum()).backward()

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import gated_deltanet_chunkwise_gdn_gb300 as gdn
-from gated_deltanet_chunkwise_gdn_gb300 import _buffers, _lib
+from gated_deltanet_chunkwise_gdn_gb300 import _buffers, _lib, mixer
 
 
 class OnGpu(torch.Tensor):
@@ -194,3 +194,37 @@ def test_inputs_off_the_current_device_are_refused(library, name):
     library.device = 0
     calls()[name](stream=STREAM)
     assert len(library.calls) == 1
+
+
+def _functions():
+    """The autograd functions with the leaves of a small call."""
+    leaf = lambda *shape: torch.ones(*shape, requires_grad=True)  # noqa: E731
+    cu, q = torch.tensor([0, 2]), lambda: leaf(2, 1, 4)  # noqa: E731
+    return dict(conv=(mixer.CausalConv, (leaf(2, 8), leaf(8, 4), leaf(8), leaf(1, 3, 8), cu)),
+                ssm=(mixer.SelectiveScan, (leaf(2, 8), leaf(2, 8), leaf(8, 4), leaf(2, 1, 4), leaf(2, 1, 4), leaf(8), leaf(2, 8),
+                                           leaf(8), leaf(1, 8, 4), cu)),
+                norm=(mixer.LayerNorm, (leaf(2, 8), leaf(8), leaf(8))),
+                delta=(gdn.GatedDeltaNetChunkwise, (q(), q(), q(), leaf(2, 1), leaf(2, 1), leaf(1), leaf(1), leaf(1, 1, 4, 4), cu)))
+
+
+@pytest.mark.parametrize("name", ["conv", "ssm", "norm", "delta"])
+def test_second_derivatives_are_refused(monkeypatch, name):
+    """The gradients come from kernels: a loss on them would miss its part in silence."""
+    zeros = lambda *ts: [torch.zeros_like(t) for t in ts]  # noqa: E731
+    monkeypatch.setattr(mixer, "gdn_conv_extend", lambda x, *a, **k: x * 2)
+    monkeypatch.setattr(mixer, "gdn_conv_backward", lambda x, w, b, p, *a, **k: gdn.GdnConvGrads(*zeros(x, w, b, p)))
+    monkeypatch.setattr(mixer, "gdn_ssm_extend", lambda x, *a, **k: x * 2)
+    monkeypatch.setattr(mixer, "gdn_ssm_backward", lambda *a, **k: gdn.GdnSsmGrads(*zeros(*a[:9])))
+    monkeypatch.setattr(mixer, "gdn_layer_norm", lambda x, *a, **k: (x * 2, x[:, 0], x[:, 0]))
+    monkeypatch.setattr(mixer, "gdn_layer_norm_backward", lambda d, x, w, *a, **k: gdn.GdnNormGrads(*zeros(x, w, w)))
+    monkeypatch.setattr(gdn, "gdn_extend_chunkwise", lambda q, *a, **k: q * 2)
+    monkeypatch.setattr(gdn, "gdn_chunkwise_backward", lambda *a, **k: gdn.GdnGrads(*zeros(*a[:8])))
+    fn, leaves = _functions()[name]
+    out = fn.apply(*leaves)
+    out = out[0] if isinstance(out, tuple) else out
+    g, = torch.autograd.grad((out * out).sum(), leaves[0], create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        (out.sum() + g.square().sum()).backward()
+    out = fn.apply(*leaves)
+    (out[0] if isinstance(out, tuple) else out).sum().backward()
+    assert all(t.grad is not None for t in leaves if t.requires_grad)
