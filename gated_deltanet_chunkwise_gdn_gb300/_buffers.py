@@ -14,18 +14,23 @@ _words: dict = {}
 UNSHARED = contextlib.nullcontext()  # in the place of a lock, for a workspace that is one call's alone
 
 
-_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+# What a call needs of CUDA on its way costs the host tenths of a microsecond a question, so the questions go straight
+# to the binding where it has them.
+current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def require_current(device: torch.device) -> None:
     """The library launches on the thread's current device: the inputs' has to be that one."""
-    if _device() != device.index:
-        raise ValueError(f"the inputs are on {device}, but the current device is cuda:{_device()}: make the call under "
-                         f"torch.cuda.device({device.index})")
+    if current_device() != device.index:
+        raise ValueError(f"the inputs are on {device}, but the current device is cuda:{current_device()}: make the call "
+                         f"under torch.cuda.device({device.index})")
 
 
-def _capturing(stream) -> bool:
-    """Whether a graph is being captured on the stream (None: the current one)."""
+def _capturing(stream, handle: int) -> bool:
+    """Whether a graph is being captured on the stream (None: the current one) of this handle. The default stream's is
+    0, and it takes no part in captures: calls there are spared the question."""
+    if handle == 0:
+        return False
     if stream is None:
         return torch.cuda.is_current_stream_capturing()
     with torch.cuda.stream(stream):
@@ -52,7 +57,7 @@ def workspace_for(device: torch.device, stream, handle: int, nbytes: int):
     replayed on any stream, beside calls on the stream that it was captured on and beside other graphs
     captured there, and after a larger call has replaced the kept buffer.
     """
-    if _capturing(stream):
+    if _capturing(stream, handle):
         return _new(nbytes + 256, torch.uint8, device, stream), UNSHARED
     key = (device.index, handle)
     lock = workspace_lock(device, handle)
@@ -101,7 +106,7 @@ def status_word(device: torch.device, stream, handle: int) -> torch.Tensor:
     that can run, or be enqueued, at the same time may have the same one; a step that is captured into a graph
     has one of the graph's own, as a workspace would be. Every step writes the word before it reads it.
     """
-    if _capturing(stream):
+    if _capturing(stream, handle):
         return _new(1, torch.int32, device, stream)
     key = (device.index, handle, threading.get_ident())
     word = _words.get(key)

@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._buffers import UNSHARED, aligned_ptr, given_workspace, require_current, status_word, workspace_for
+from ._buffers import UNSHARED, aligned_ptr, current_device, given_workspace, require_current, status_word, workspace_for
 from ._lib import GdnError
 
 _DTYPE_CODE = {torch.bfloat16: _lib.GDN_BF16, torch.float16: _lib.GDN_FP16, torch.float32: _lib.GDN_FP32}
@@ -101,9 +101,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
 
 def _stream(stream, dev):
     """(the given stream or None, handle of the stream to run on), where the inputs' device is the current one."""
-    require_current(dev)
+    index = dev.index
+    if current_device() != index:
+        require_current(dev)
     if stream is None:
-        return None, _raw_stream(dev.index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+        return None, _raw_stream(index) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=dev)
     return stream, stream.cuda_stream

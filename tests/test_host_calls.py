@@ -61,7 +61,8 @@ def library(monkeypatch):
         monkeypatch.setattr(torch, new, on_gpu)
     lib.capturing = False
     lib.device = 0
-    monkeypatch.setattr(_buffers, "_device", lambda: lib.device)
+    for module in (_buffers, mixer):
+        monkeypatch.setattr(module, "current_device", lambda: lib.device)
     monkeypatch.setattr(torch, "zeros_like", lambda t: on_gpu(*t.shape, dtype=t.dtype))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: lib.capturing)
     for cache in ("_workspaces", "_locks", "_words"):
