@@ -340,7 +340,8 @@ def gdn_get_device_status(device=None, stream=None) -> int:
 
 
 class KernelProfile:
-    """Per-kernel device time of the library's launches between start() and stop().
+    """Per-kernel device time of the delta rule's launches (gdn_extend_chunkwise, gdn_decode_step,
+    gdn_chunkwise_backward) between start() and stop(). The layers around it are counted by :func:`launch_count` only.
 
     Each kernel is bracketed by CUDA events on the stream it is launched on.
     """

@@ -177,7 +177,12 @@ __device__ __forceinline__ void ring_wait() {  // all but the last N committed g
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float ex2(float x) {  // 2^x by the special-function unit
+// 2^x and 1 / x by the special-function unit, for every type: relative error about 2^-22 and 2^-23, results under 2^-126 zero.
+// Beside them stands the argument's own rounding, 2^-24 of it, which the exact functions could not take back. The
+// scan forms one exponential a state and token and is bound by them; where a tie of a 16-bit rounding is that near, an
+// output falls on its other side (7 of 327680 values of single-token convolutions are not the nearest bf16, and 5 of those of
+// elementary torch operations in fp32).
+__device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;

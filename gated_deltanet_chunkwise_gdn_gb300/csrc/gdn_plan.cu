@@ -162,7 +162,7 @@ SegmentRule segment_rule(int64_t T, int B, int unit, int least, int64_t target) 
   SegmentRule r{};
   r.unit = unit;
   r.least = least;
-  if (B > kPlanThreads) {  // sequences enough to fill the card: not cut at all
+  if (B > kPlanThreads) {  // not cut at all: sequences enough to fill the card, unless most tokens are in a few of them
     r.least = (int)(T > least ? T : least);
   } else {
     r.target = (int)(target < (1 << 20) ? target : (1 << 20));

@@ -22,10 +22,15 @@
 // The passes are bound by instruction latency and the shared-memory pipe: about 19 operations and 3
 // exponentials a state and token, issued in 0.54 of the cycles by 2.7 warps a scheduler, with 0.57 of the
 // shared-memory pipe's rate. 3 x 4096 tokens x 2048 channels x 16 states in bf16: local 207 us, main 589, carry
-// 12, sum 16 (the rows' bytes alone would take 45). The layout is chosen for the arithmetic: a thread owns CPT channels x S states, B and C come as broadcasts from
-// shared memory, sums over states take few shuffles (each lane ends up with one channel's sum), and
-// sums over channels are first taken inside the thread and then by one tensor-core product with a
-// matrix of ones: the value split in its upper 11 bits and the rest, both exact to 22 bits in tf32.
+// 12, sum 16 (the rows' bytes alone would take 45). The layout is chosen for the arithmetic: a thread owns CPT channels
+// x S states, B and C come as broadcasts from shared memory, sums over states take few shuffles (each lane ends up with
+// one channel's sum), and sums over channels are first taken inside the thread in fp32 and then by one tensor-core
+// product with a matrix of ones. tf32 holds 11 bits, so a thread's sum goes in as its upper 11 bits and the next 11: the
+// last two of fp32's 24 are dropped, an error of at most 2^-22 of a thread's sum, for every type. Where a third product
+// would keep them, it would cost as much as either of the two; the sum's own order already moves results by that much.
+//
+// An infinite input leaves NaN, where the formulas have an infinity, in ddt and dz of its channel from its token on, if the
+// states do not fill their lanes (a padded state multiplies it by zero).
 #include "gdn_ssm.cuh"
 
 namespace gdn {
@@ -43,8 +48,11 @@ struct BwdMap {
   static constexpr int CW = CL * CPT;            // channels of a warp
   static constexpr int kChannels = CW * kWarps;  // of a block
   static constexpr int kStates = S * NL;
-  // Blocks on an SM: 168 registers a thread, 77 KB of shared memory. 3 x 4096 tokens x 2048 channels, forward and
-  // backward, take 1040 us with three, 1146 with two. (Four would leave a thread two channels: slower too.)
+  // Blocks on an SM: 168 registers a thread allow three. 3 x 4096 tokens x 2048 channels x 16 states in bf16, forward and
+  // backward, take 1040 us with three, 1146 with two. (Four would leave a thread two channels: slower too.) Shared
+  // memory allows three up to 8 states, and up to 32 for 16-bit rows read in pairs (sizeof(MainSmem) 54 to 76 KB).
+  // For fp32 and for single 16-bit columns it is 92160 bytes with 9 to 16 states and 77824 with 17 to 32, and above 32
+  // states 81920 to 86016 for every type: two blocks fit, while the segments are still cut for three.
   static constexpr int kBlocks = 3;
   static_assert(CL >= 4, "the product with ones takes four lanes of one state lane at a time");
 };

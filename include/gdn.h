@@ -266,7 +266,8 @@ GDN_API gdn_status gdn_chunkwise_backward(const void *q, const void *k, const vo
  * rows and channel counts run on the wide loads. Packed batches, slots, streams and errors are as for gdn_extend_chunkwise above: bad
  * cu_seqlens or cache_indices are found on the device, the call's later kernels then do nothing, and
  * the status is read with gdn_get_device_status from the workspace (or the step's status word).
- * Sums over tokens, rows or channels are taken in a fixed order: equal calls give equal bits.
+ * Sums over tokens, rows or channels are taken in a fixed order: equal calls give equal bits. Exponentials and
+ * reciprocals are the special-function unit's (about 2^-22), whatever the dtype.
  * No output may overlap an input, except where said. No call allocates. Where a 16-bit activation of
  * the scan starts in the middle of an aligned 4-byte word, the word's first half, the element before the
  * array, is read too and dropped: it has to be readable, as it is in any allocation of 4-byte alignment.
@@ -471,9 +472,10 @@ GDN_API gdn_status gdn_test_set_stall(int32_t kernel, int64_t wait_budget_cycles
 GDN_API const char *gdn_status_string(gdn_status status);
 
 /*
- * Instrumentation. gdn_profile_start makes every later gdn_extend_chunkwise or gdn_decode_step call
- * record a pair of CUDA events around each kernel it launches, on the call's own
- * stream, for up to max_launches kernel launches in total (the events are created
+ * Instrumentation. gdn_profile_start makes every later gdn_extend_chunkwise, gdn_decode_step or
+ * gdn_chunkwise_backward call (not the layers around the delta rule) record a pair of
+ * CUDA events around each kernel or kernel group it launches, on the call's own
+ * stream, for up to max_launches of them in total (the events are created
  * here, on the current device). gdn_profile_stop waits for those events, adds the
  * elapsed time of each kernel kind into total_ms[id] and its launch count into
  * launches[id] for id < n_slots, frees the events and returns the number of kernel
