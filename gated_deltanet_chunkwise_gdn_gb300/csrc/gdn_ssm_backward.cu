@@ -29,8 +29,8 @@
 // last two of fp32's 24 are dropped, an error of at most 2^-22 of a thread's sum, for every type. Where a third product
 // would keep them, it would cost as much as either of the two; the sum's own order already moves results by that much.
 //
-// An infinite input leaves NaN, where the formulas have an infinity, in ddt and dz of its channel from its token on, if the
-// states do not fill their lanes (a padded state multiplies it by zero).
+// Where the states do not fill their lanes, an infinite input or output gradient can leave NaN, where the formulas have an
+// infinity, in the gradients of its own channel: a padded state multiplies it by zero.
 #include "gdn_ssm.cuh"
 
 namespace gdn {
